@@ -6,7 +6,8 @@
 // s_b, exact in f16) and takes the partial dots with every query; lane r of the warp
 // puts them into CTA r's table (distributed shared memory), and one cluster barrier
 // later every CTA sums the tables, forms the weights and mixes its own channels from
-// the decoded rows.  One round trip to memory, one to the cluster.  One token, 4
+// the decoded rows.  One round trip to memory, one to the cluster (and before it a wait until
+// every CTA runs, which the first source's loads cover).  One token, 4
 // queries, 8 FP4 sources, d = 4096: 15.1 us in the streaming kernel (one CTA), 5.0 here.
 #include "depth_cache.cuh"
 #include "dispatch.h"
@@ -30,6 +31,8 @@ __global__ void __launch_bounds__(CACHE_FEW_THREADS) cache_read_few_kernel(const
     float *tails = wt + NQ * n_src;                                         // [n_src][2]: row scale, sum of squares
     uint32_t rank;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    cluster_arrive_started();
+    bool started = false;
     const int64_t t = blockIdx.x / cs;
     const int u0 = (int)rank * U, uph = d / 16 / H, head = u0 / uph;
     const unsigned char *tok = a.r.cache + t * a.r.row.bytes;
@@ -64,6 +67,8 @@ __global__ void __launch_bounds__(CACHE_FEW_THREADS) cache_read_few_kernel(const
                     }
             }
         }
+        if (!started) cluster_wait_started();
+        started = true;
 #pragma unroll
         for (int q = 0; q < NQ; ++q) {
             const float s = seg_sum<32>(dot[q].x + dot[q].y);
@@ -72,6 +77,7 @@ __global__ void __launch_bounds__(CACHE_FEW_THREADS) cache_read_few_kernel(const
                              : "memory");
         }
     }
+    if (!started) cluster_wait_started();      // (a warp without a source)
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 
     // weights: one warp per query; the partial dots of the CTAs that share this CTA's head

@@ -59,6 +59,14 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
     return ok != 0;
 }
 
+// That CTAs of a cluster are scheduled together does not say that they run yet, and until a CTA
+// does, no other may touch its shared memory: every thread arrives at the start of the kernel and
+// waits before its CTA's first access to another's, with work of its own between the two.  Whole warps.
+__device__ __forceinline__ void cluster_arrive_started() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait_started() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+
 // Waits for phase `parity` of `bar` to complete.  Gives up when `abort_flag`
 // (CTA shared memory) becomes nonzero or after cfg.timeout_ns; on a timeout
 // it records DEV_ERR_TIMEOUT in the device status word and raises the CTA's
