@@ -9,8 +9,8 @@
 // `rank` holds the 16-byte vectors [rank*vpc, (rank+1)*vpc) of every source,
 // one vector per thread, straight in registers (no staging); the per-source
 // sums of squares and query dots are reduced by a warp butterfly, a shared
-// table and one exchange through distributed shared memory; after the single
-// cluster barrier every CTA has the totals, computes the softmax and writes its
+// table and one exchange through distributed shared memory; after the
+// cluster barrier behind it every CTA has the totals, computes the softmax and writes its
 // slice of the outputs.
 #pragma once
 
@@ -65,6 +65,7 @@ __global__ void __launch_bounds__(DEC_MAX_THREADS) depth_read_decode_kernel(cons
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int nw = blockDim.x >> 5;
     const int rank = (int)cluster.block_rank();
+    cluster_arrive_started();
     const int64_t t = blockIdx.x / a.cs;
     const int vec = rank * a.vpc + tid;              // this thread's 16-byte vector of the row
     const int c0 = vec * EPV;
@@ -115,7 +116,8 @@ __global__ void __launch_bounds__(DEC_MAX_THREADS) depth_read_decode_kernel(cons
         if (idx >= 0) red[warp * V + idx] = v[j];
     }
     __syncthreads();
-    // this CTA's totals, sent to every CTA of the cluster (itself included)
+    // this CTA's totals, sent to every CTA of the cluster (itself included) once all of them run
+    cluster_wait_started();
     for (int j = tid; j < V; j += blockDim.x) {
         float s = 0.f;
         for (int w = 0; w < nw; ++w) s += red[w * V + j];

@@ -24,7 +24,8 @@ def kernels(name):
         yield re.findall(r"(\w+)\s*\(", m.group(1))[-1], text[m.end():at]
 
 
-@pytest.mark.parametrize("name", ["cache_read_few.cu", "cache_read_mma.cuh", "msar.cu", "msar_phase1.cu", "msar_tile.cu"])
+@pytest.mark.parametrize("name", ["cache_read_few.cu", "cache_read_mma.cuh", "depth_read_decode.cuh", "msar.cu",
+                                  "msar_phase1.cu", "msar_tile.cu"])
 def test_no_write_into_a_cta_that_may_not_run_yet(name):
     """A CTA's shared memory may be written by others of its cluster only once it runs, and being
     scheduled with them does not say so: a cluster wait comes before the first such write."""
