@@ -446,8 +446,8 @@ def attnres_debug_set_wait_timeout_ns(ns: int):
     load().attnres_debug_set_wait_timeout_ns(int(ns))
 
 
-def attnres_debug_set_stall_injection(enable: bool):
-    load().attnres_debug_set_stall_injection(1 if enable else 0)
+def attnres_debug_set_stall_injection(enable: int):
+    load().attnres_debug_set_stall_injection(int(enable))
 
 
 def attnres_debug_set_kernel_variant(variant: int):

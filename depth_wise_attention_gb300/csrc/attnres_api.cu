@@ -3321,7 +3321,7 @@ void attnres_debug_set_wait_timeout_ns(uint64_t ns) {
     g_timeout_ns.store(ns ? ns : 2000000000ull);
 }
 
-void attnres_debug_set_stall_injection(int enable) { g_inject_stall.store(enable ? 1 : 0); }
+void attnres_debug_set_stall_injection(int enable) { g_inject_stall.store(enable > 0 ? enable : enable ? 1 : 0); }
 
 void attnres_debug_set_kernel_variant(int variant) {
     g_kernel_variant.store(variant >= 1 && variant <= 3 ? variant : 0);

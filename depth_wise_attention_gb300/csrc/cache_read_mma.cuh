@@ -120,8 +120,11 @@ inline uint32_t cm_barriers(uint32_t pitch, uint32_t rs, int heads, int cs) {
 inline uint32_t cm_stage_bytes(uint32_t pitch, uint32_t rs, int heads, int cs) {
     return (cm_barriers(pitch, rs, heads, cs) + 32 + 16 * (uint32_t)heads + 127) / 128 * 128;
 }
-// Behind the stages: the abort flag, and K2's running state [H][3][4].
-inline uint32_t cm_aux_bytes(int heads) { return 16 + 48 * (uint32_t)heads; }
+// Behind the stages: the abort flag; CL: per head shared with other CTAs (index as in sums) the
+// items whose sums this CTA has sent, [2] tokens or halves each, and has armed its barrier for; and
+// K2's running state [H][3][4].
+constexpr uint32_t CM_SENT = 16, CM_ARMED = 32, CM_STATE = 48;
+inline uint32_t cm_aux_bytes(int heads) { return CM_STATE + 48 * (uint32_t)heads; }
 
 // First unit of slice i of a head that begins at unit u0; it and the 15 units after it
 // lie in the row where that can be (else the row has zeros behind it in the stage).
@@ -211,6 +214,15 @@ __device__ __forceinline__ int cm_aborted(uint32_t flag) {
     asm volatile("ld.volatile.shared.s32 %0, [%1];" : "=r"(v) : "r"(flag));
     return v;
 }
+// Raises the abort flag of every CTA of the cluster (this one's alone where there is none): what a
+// CTA that gave up would have sent the others never comes, and they must not take anything else for it.
+__device__ __forceinline__ void cm_abort(uint32_t flag) {
+    uint32_t n;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
+    for (uint32_t r = 0; r < n; ++r)
+        asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, %1;\n"
+                     " st.relaxed.cluster.shared::cluster.u32 [a], %2;\n}\n" ::"r"(flag), "r"(r), "r"(1) : "memory");
+}
 // mbar_wait_bounded, with 64 tries between looks at the clock: the hand-overs here
 // are waited for in every item, and reading the clock takes longer than most waits.
 // HEED: give up at once when another warp has.
@@ -225,7 +237,7 @@ __device__ __forceinline__ bool cm_wait(uint32_t bar, uint32_t parity, uint32_t 
             if (t0 == 0) t0 = now;
             if (now - t0 > cfg.timeout_ns) {
                 atomicOr(cfg.status, DEV_ERR_TIMEOUT);
-                asm volatile("st.volatile.shared.s32 [%0], 1;" ::"r"(flag) : "memory");
+                cm_abort(flag);
                 return false;
             }
         }
@@ -579,7 +591,7 @@ __device__ __forceinline__ void cm_init_barriers(const CacheReadMmaArgs &a, uint
         cm_bar_init(b + 16 + 8 * h, nl < 1 ? 1 : nl);
         cm_bar_init(b + 16 + 8 * (H + h), nl < 1 ? 1 : nl < per_item ? nl : per_item);
     }
-    if (tid == 0) asm volatile("st.volatile.shared.s32 [%0], 0;" ::"r"(flag) : "memory");
+    if (tid < (int)CM_STATE / 4) asm volatile("st.volatile.shared.s32 [%0], 0;" ::"r"(flag + 4 * tid) : "memory");
     mbar_init_fence();
 }
 
@@ -620,17 +632,6 @@ __device__ __forceinline__ void cm_cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// No CTA leaves while another may still write into it.  A CTA that waited for everything that
-// was sent to it has nothing on its way; one that gave up may have, for the microseconds
-// that a store takes.
-__device__ __forceinline__ void cm_leave_cluster(uint32_t flag, int tid) {
-    if (tid == 0 && cm_aborted(flag)) {
-        const uint64_t t0 = globaltimer_ns();
-        while (globaltimer_ns() - t0 < 100000) {}
-    }
-    cm_cluster_sync();
-}
-
 // Leaves a warp's partial dots of 16 rows at `at` (rows g) and 128 rs further (g + 8).
 __device__ __forceinline__ void cm_leave_dots(const CacheReadMmaArgs &a, uint32_t at, uint32_t bar, float dot0, float dot1,
                                               int lane) {
@@ -644,11 +645,16 @@ __device__ __forceinline__ void cm_leave_dots(const CacheReadMmaArgs &a, uint32_
 struct CMShare {
     int r0, r1, slot;
 };
-// Sends this CTA's sum of value 32 k + lane to the head's other CTAs; it reports to their
-// barriers when it has landed.
-__device__ __forceinline__ void cm_send_sum(const CacheReadMmaArgs &a, const CMSlice &s, const CMShare &sh, uint32_t st, int k,
-                                            float v, int lane) {
+__device__ __forceinline__ void cm_count(uint32_t a, int v) {
+    asm volatile("st.volatile.shared.s32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+// Sends this CTA's sum of value 32 k + lane of an item to the head's other CTAs; it reports to their
+// barriers when it has landed.  Only a CTA that has not given up does: no warp adds to the sums
+// or arrives at a barrier before its turn unless the flag was up first.
+__device__ __forceinline__ void cm_send_sum(const CacheReadMmaArgs &a, const CMSlice &s, const CMShare &sh, uint32_t st, int item,
+                                            int k, float v, uint32_t flag, int lane) {
     const int H = a.r.row.H;
+    if (lane == 0 && sh.r1 > sh.r0) cm_count(flag + CM_SENT + 4 * (2 * sh.slot + k), item + 1);
     for (int r = sh.r0; r <= sh.r1; ++r) {
         if (r == s.rank) continue;
         const int slot = s.head * a.wph < r * a.nw ? 0 : 1;
@@ -661,10 +667,13 @@ __device__ __forceinline__ void cm_send_sum(const CacheReadMmaArgs &a, const CMS
     }
 }
 // The one arrival of a sums barrier: 64 values from each other CTA of the head.
-__device__ __forceinline__ void cm_expect_sums(const CacheReadMmaArgs &a, const CMShare &sh, uint32_t st, int lane) {
-    if (lane == 0 && sh.r1 > sh.r0)
+__device__ __forceinline__ void cm_expect_sums(const CacheReadMmaArgs &a, const CMShare &sh, uint32_t st, int item, uint32_t flag,
+                                               int lane) {
+    if (lane == 0 && sh.r1 > sh.r0) {
+        cm_count(flag + CM_ARMED + 4 * sh.slot, item + 1);
         asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
                      ::"r"(st + a.bars + 16 + 16 * a.r.row.H + 8 * sh.slot), "r"(256 * (sh.r1 - sh.r0)) : "memory");
+    }
 }
 // The head's sum of value 32 k + lane, always in the same order.
 __device__ __forceinline__ float cm_all_sums(const CacheReadMmaArgs &a, const CMSlice &s, const CMShare &sh, uint32_t st, int k,
@@ -673,6 +682,48 @@ __device__ __forceinline__ float cm_all_sums(const CacheReadMmaArgs &a, const CM
     for (int r = sh.r0; r <= sh.r1; ++r)
         sum += r == s.rank ? v : lds32f(st + a.bars - 512 * a.cs + (uint32_t)((sh.slot * a.cs + r) * 64 + 32 * k + lane) * 4);
     return sum;
+}
+
+// The end of a cluster: no CTA leaves while another may still write into it.  Where none gave up, each
+// has waited for all that was sent to it.  Otherwise (every flag is up then) sums may be on their way:
+// of a head's last armed item, or of the one after it, for a CTA sends an item's only when it has
+// the others' of the item before.  Their number is what the senders counted, so the barriers of
+// these two items are made to complete when they have landed.
+__device__ __forceinline__ void cm_leave_cluster(const CacheReadMmaArgs &a, int rank, uint32_t stage0, uint32_t flag, int tid) {
+    cm_cluster_sync();
+    if (!cm_aborted(flag)) return;
+    if (tid == 0)
+        for (int slot = 0; slot < 2; ++slot) {
+            const int first = rank * a.nw, head = (slot == 0 ? first : first + a.nw - 1) / a.wph, s0 = head * a.wph;
+            const int r0 = s0 / a.nw, r1 = (s0 + a.wph - 1) / a.nw;
+            if ((s0 < first ? 0 : 1) != slot || r1 == r0) continue;
+            const int armed = cm_aborted(flag + CM_ARMED + 4 * slot);
+            for (int item = armed > 0 ? armed - 1 : 0; item <= armed; ++item) {
+                uint32_t bytes = 0;
+                for (int r = r0; r <= r1; ++r)
+                    for (int k = 0; k < 2 && r != rank; ++k) {
+                        const uint32_t at = flag + CM_SENT + 4 * (2 * (s0 < r * a.nw ? 0 : 1) + k);
+                        int sent;
+                        asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %1, %2;\n"
+                                     " ld.relaxed.cluster.shared::cluster.s32 %0, [a];\n}\n"
+                                     : "=r"(sent) : "r"(at), "r"(r) : "memory");
+                        if (sent > item) bytes += 128;
+                    }
+                const uint32_t bar = stage0 + item % a.nstages * a.stage_bytes + a.bars + 16 + 16 * a.r.row.H + 8 * slot;
+                if (item < armed) {
+                    const uint32_t never = 256 * (uint32_t)(r1 - r0) - bytes;
+                    if (never)
+                        asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(never)
+                                     : "memory");
+                } else if (bytes) {
+                    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+                } else {
+                    continue;
+                }
+                cm_wait<true, false>(bar, (uint32_t)(item / a.nstages) & 1, flag, a.wait);
+            }
+        }
+    cm_cluster_sync();
 }
 
 // A position in the ring of stages.
@@ -693,10 +744,11 @@ struct CMRefill {
     int turn;           // iterations until this warp's next refill
     int last = -1;      // the last item that it issued
     bool on;
+    // (a test may stop all copies, 1, or those of the CTA of rank r behind its first items, 2 + r)
     template <typename F>
-    __device__ __forceinline__ CMRefill(const CacheReadMmaArgs &a, uint32_t stage0, int warp, int n_items, const F &issue)
-        : turn(warp), on(!a.wait.inject_stall) {
-        if (warp == 0 && on)
+    __device__ __forceinline__ CMRefill(const CacheReadMmaArgs &a, uint32_t stage0, int rank, int warp, int n_items, const F &issue)
+        : turn(warp), on(a.wait.inject_stall == 0 || (a.wait.inject_stall > 1 && a.wait.inject_stall != 2 + rank)) {
+        if (warp == 0 && a.wait.inject_stall != 1)
             for (int i = 0; i < n_items && i < a.nstages; ++i) issue(i, stage0 + i * a.stage_bytes);
     }
     // r2: the position of item it - lag
@@ -724,7 +776,7 @@ struct CMRefill {
         if (lane != 0 || !cm_aborted(flag)) return;
         for (int i = last; i >= 0 && i > last - a.nstages; i -= a.nw)
             cm_wait<false, false>(stage0 + i % a.nstages * a.stage_bytes + a.bars, (uint32_t)(i / a.nstages) & 1, flag, a.wait);
-        if (warp == 0 && !a.wait.inject_stall)
+        if (warp == 0 && a.wait.inject_stall != 1)
             for (int i = 0; i < n_items && i < a.nstages; ++i)
                 cm_wait<false, false>(stage0 + i * a.stage_bytes + a.bars, 0, flag, a.wait);
     }
@@ -821,7 +873,7 @@ __global__ void __launch_bounds__(CM_MAX_WARPS * 32, 1) cache_read_mma_kernel(co
             cm_copy_row<FMT>(a, plan, sl.rank, stage + (size_t)lane * a.pitch,
                              a.r.cache + (t0 + k) * a.r.row.bytes + (int64_t)i * a.r.cache_stride_bytes, full, pol);
     };
-    CMRefill rf(a, stage0, warp, n_items, issue);
+    CMRefill rf(a, stage0, sl.rank, warp, n_items, issue);
 
     uint32_t bq[16][2];
     const float qinv = cm_query_fragments<FMT>(a.r, sl.chan, sl.mask, g, c, bq);
@@ -879,6 +931,7 @@ __global__ void __launch_bounds__(CM_MAX_WARPS * 32, 1) cache_read_mma_kernel(co
             const bool forms0 = turn == 0, forms1 = turn == (nl > 1 ? 1 : 0);
             if (forms0 || forms1) {
                 cm_wait(r1.base + dots_in, r1.par, flag, a.wait);
+                const bool send = CL && !__any_sync(0xffffffffu, cm_aborted(flag));
                 float dt[2];
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
@@ -886,13 +939,13 @@ __global__ void __launch_bounds__(CM_MAX_WARPS * 32, 1) cache_read_mma_kernel(co
                         const uint32_t d = r1.base + CM_ROWS * a.pitch + (uint32_t)((k * 32 + lane) * a.rs) * 4;
                         if constexpr (CL) {
                             dt[k] = cm_sum_warps(d + (warp - sl.local) * 4, nl);
-                            cm_send_sum(a, sl, share, r1.base, k, dt[k], lane);
+                            if (send) cm_send_sum(a, sl, share, r1.base, it, k, dt[k], flag, lane);
                         } else {
                             dt[k] = cm_sum(d + head * a.wpc * 4, a.wpc);
                         }
                     }
-                if (CL && share.r1 > share.r0) {
-                    if (forms0) cm_expect_sums(a, share, r1.base, lane);
+                if (send && share.r1 > share.r0) {
+                    if (forms0) cm_expect_sums(a, share, r1.base, it, flag, lane);
                     cm_wait<CL>(r1.base + a.bars + 16 + 16 * H + 8 * share.slot, r1.par, flag, a.wait);
                 }
 #pragma unroll
@@ -912,7 +965,7 @@ __global__ void __launch_bounds__(CM_MAX_WARPS * 32, 1) cache_read_mma_kernel(co
         }
     }
     rf.drain(a, stage0, warp, lane, n_items, flag);
-    if constexpr (CL) cm_leave_cluster(flag, tid);
+    if constexpr (CL) cm_leave_cluster(a, sl.rank, stage0, flag, tid);
 }
 
 // Weights of 16 rows (one item) of a token and head, and the factor by which what
@@ -1027,7 +1080,7 @@ __global__ void __launch_bounds__(CM_MAX_WARPS * 32, 1) cache_read_mma_multi_ker
                              a.r.cache + (bid + (int64_t)tok * gstride) * a.r.row.bytes +
                                  (int64_t)(i0 + (lane < rows ? lane : rows - 1)) * a.r.cache_stride_bytes, full, pol);
     };
-    CMRefill rf(a, stage0, warp, n_items, issue);
+    CMRefill rf(a, stage0, sl.rank, warp, n_items, issue);
 
     uint32_t bq[16][2];
     const float qinv = cm_query_fragments<FMT>(a.r, sl.chan, sl.mask, g, c, bq);
@@ -1105,26 +1158,27 @@ __global__ void __launch_bounds__(CM_MAX_WARPS * 32, 1) cache_read_mma_multi_ker
                     cm_wait((wrap ? flag : r1.base) - a.stage_bytes + weights_in, r1.par ^ (wrap ? 1u : 0u), flag, a.wait);
                 }
                 cm_wait(r1.base + dots_in, r1.par, flag, a.wait);
+                const bool send = CL && !__any_sync(0xffffffffu, cm_aborted(flag));
                 float dt[2];
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const uint32_t d = r1.base + CM_ROWS * a.pitch + (uint32_t)((k * 32 + lane) * a.rs) * 4;
                     if constexpr (CL) {
                         dt[k] = cm_sum_warps(d + (warp - sl.local) * 4, nl);
-                        cm_send_sum(a, sl, share, r1.base, k, dt[k], lane);
+                        if (send) cm_send_sum(a, sl, share, r1.base, it, k, dt[k], flag, lane);
                     } else {
                         dt[k] = cm_sum(d + head * a.wpc * 4, a.wpc);
                     }
                 }
                 if constexpr (CL) {
-                    if (share.r1 > share.r0) {
-                        cm_expect_sums(a, share, r1.base, lane);
+                    if (send && share.r1 > share.r0) {
+                        cm_expect_sums(a, share, r1.base, it, flag, lane);
                         cm_wait<CL>(r1.base + a.bars + 16 + 16 * H + 8 * share.slot, r1.par, flag, a.wait);
                     }
 #pragma unroll
                     for (int k = 0; k < 2; ++k) dt[k] = cm_all_sums(a, sl, share, r1.base, k, dt[k], lane);
                 }
-                cm_form16<LO>(a, r1.base, head, t, chunk, chunk == nchunks - 1, dt, inv_dh, lane, lse, flag + 16 + 48 * head,
+                cm_form16<LO>(a, r1.base, head, t, chunk, chunk == nchunks - 1, dt, inv_dh, lane, lse, flag + CM_STATE + 48 * head,
                               flag);
                 __syncwarp();
                 if (lane == 0) cm_arrive(r1.base + weights_in);
@@ -1135,7 +1189,7 @@ __global__ void __launch_bounds__(CM_MAX_WARPS * 32, 1) cache_read_mma_multi_ker
         }
     }
     rf.drain(a, stage0, warp, lane, n_items, flag);
-    if constexpr (CL) cm_leave_cluster(flag, tid);
+    if constexpr (CL) cm_leave_cluster(a, sl.rank, stage0, flag, tid);
 }
 
 }  // namespace attnres

@@ -16,7 +16,7 @@ enum : int { DEV_ERR_TIMEOUT = 1 };
 struct WaitCfg {
     int *status;            // device status word (bit DEV_ERR_TIMEOUT)
     uint64_t timeout_ns;    // limit of one wait
-    int inject_stall;       // nonzero: producers issue no copies (test hook)
+    int inject_stall;       // nonzero: producers issue no copies (test hook; above 1 see attnres.h)
 };
 
 __device__ __forceinline__ uint64_t globaltimer_ns() {

@@ -911,7 +911,10 @@ attnres_status_t attnres_sync_status(void *stream);
  * attnres_debug_set_stall_injection: when nonzero, kernels that stage data
  *   with bulk copies issue no copies, so their first wait can only end by
  *   running out of time; they then record ATTNRES_ERR_TIMEOUT and return
- *   without touching memory.  Applies to launches made after the call.
+ *   without touching memory.  Applies to launches made after the call.  2 + r:
+ *   a quantised read that runs on clusters stops the copies of one CTA in each
+ *   only, that of rank r, and only behind its first items; the outputs that it
+ *   writes before it gives up are right.
  */
 void attnres_debug_set_wait_timeout_ns(uint64_t ns);
 void attnres_debug_set_stall_injection(int enable);

@@ -38,3 +38,18 @@ def test_no_write_into_a_cta_that_may_not_run_yet(name):
         wait = re.search(WAIT, body)
         assert wait is not None and wait.start() < first.start(), kernel
     assert found
+
+
+def test_sums_are_sent_by_a_cta_that_has_not_given_up():
+    """A CTA of the tensor-core read of quantised rows that gave up runs on without waiting; what it would send the
+    others then belongs to no item that they wait for.  And the last cluster barrier alone does not say that
+    what was sent has landed."""
+    for kernel, body in kernels("cache_read_mma.cuh"):
+        for m in re.finditer(r"cm_send_sum\(", body):
+            assert body[:m.start()].rstrip().endswith("if (send)"), kernel
+        send = re.search(r"const bool send = ([^;]*);", body)
+        assert send is not None and "cm_aborted(flag)" in send.group(1), kernel
+    text = open(os.path.join(CSRC, "cache_read_mma.cuh")).read()
+    leave = text[text.index("void cm_leave_cluster("):]
+    leave = leave[:leave.index("\n}\n")]
+    assert leave.count("cm_cluster_sync();") == 2 and "globaltimer" not in leave
