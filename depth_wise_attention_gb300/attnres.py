@@ -5,6 +5,11 @@ kernels.  Tensors are torch CUDA tensors (torch supplies device memory and the
 current stream); each function has the name of the C entry point it calls and
 raises ``AttnResError`` when the call does not return ATTNRES_OK.  There is no
 fallback: if the library is missing, the first call raises.
+
+``stream``: the stream of the call's kernels instead of the current one, as if the
+call were made under ``torch.cuda.stream(stream)``: outputs and workspaces that it
+allocates belong to that stream too.  The caller orders it with the streams that
+write the inputs and use the outputs.
 """
 from __future__ import annotations
 
@@ -12,6 +17,7 @@ import collections
 import contextlib
 import ctypes
 import functools
+import inspect
 import os
 import re
 
@@ -171,6 +177,34 @@ def _stream(stream):
     return _vp(s.cuda_stream)
 
 
+def _on_stream(fn):
+    """Runs fn under the `stream` that it is given.  Memory of the caching allocator goes by the stream that is
+    current when it is allocated: what fn allocates on another stream than that of its kernels could still be in
+    use there, and would be handed out again there while the kernels use it."""
+    at = list(inspect.signature(fn).parameters).index("stream")
+
+    @functools.wraps(fn)
+    def call(*args, **kw):
+        stream = args[at] if len(args) > at else kw.get("stream")
+        if stream is None:
+            return fn(*args, **kw)
+        import torch
+        dev = stream.device_index
+        if dev != torch._C._cuda_getDevice():
+            with torch.cuda.stream(stream):
+                return fn(*args, **kw)
+        # what that context does on the current device, at a tenth of its 10 us
+        before = torch._C._cuda_getCurrentStream(dev)
+        if before[0] == stream.stream_id:
+            return fn(*args, **kw)
+        torch._C._cuda_setStream(stream_id=stream.stream_id, device_index=dev, device_type=stream.device_type)
+        try:
+            return fn(*args, **kw)
+        finally:
+            torch._C._cuda_setStream(stream_id=before[0], device_index=before[1], device_type=before[2])
+    return call
+
+
 def _check(fn, status):
     if status != OK:
         raise AttnResError(fn, status)
@@ -184,6 +218,7 @@ def _src_geometry(src):
     return n_src, T, d, src.stride(0)
 
 
+@_on_stream
 def attnres_full_fwd(src, query, gain=None, eps=1e-6, out=None, stream=None):
     """Full AttnRes read of one layer: src [n_src,T,d] -> out [T,d]."""
     import torch
@@ -195,6 +230,7 @@ def attnres_full_fwd(src, query, gain=None, eps=1e-6, out=None, stream=None):
     return out
 
 
+@_on_stream
 def attnres_block_phase1(src, queries, gain=None, eps=1e-6, o=None, lse=None, want_lse=True,
                          stream=None):
     """Phase 1: queries [n_q,d] against src [n_src,T,d] -> (o [n_q,T,d], lse [n_q,T])."""
@@ -211,6 +247,7 @@ def attnres_block_phase1(src, queries, gain=None, eps=1e-6, o=None, lse=None, wa
     return o, lse
 
 
+@_on_stream
 def attnres_block_phase2_merge(o, lse, partial, query, gain=None, eps=1e-6, out=None, stream=None):
     """Phase 2: merge partial [T,d] (or None) into (o [T,d], lse [T]) -> out [T,d]."""
     import torch
@@ -223,6 +260,7 @@ def attnres_block_phase2_merge(o, lse, partial, query, gain=None, eps=1e-6, out=
     return out
 
 
+@_on_stream
 def attnres_block_phase2_update_merge(partial, f, o, lse, query, gain=None, eps=1e-6, partial_out=None,
                                       out=None, stream=None):
     """Fused update and merge: partial [T,d] or None, f [T,d] -> (partial + f, merged out).
@@ -239,6 +277,7 @@ def attnres_block_phase2_update_merge(partial, f, o, lse, query, gain=None, eps=
     return partial_out, out
 
 
+@_on_stream
 def mhar_phase2_merge(o, lse, partial, query, gain=None, eps=1e-6, f=None, partial_out=None, out=None,
                       stream=None):
     """Per-head phase-2 merge: o [T,d], lse [H,T], partial [T,d] or None, query [H,d/H].
@@ -266,6 +305,7 @@ def attnres_read_bwd_workspace_size(n_src, T, d, n_q, dtype):
     return n.value
 
 
+@_on_stream
 def attnres_read_bwd(src, queries, dout, gain=None, eps=1e-6, dsrc=None, accumulate=False, dqueries=None,
                      dgain=None, want_dgain=True, workspace=None, stream=None):
     """Backward of the read of queries [n_q,d] over src [n_src,T,d] for output
@@ -291,6 +331,7 @@ def attnres_read_bwd(src, queries, dout, gain=None, eps=1e-6, dsrc=None, accumul
     return dsrc, dqueries, dgain
 
 
+@_on_stream
 def attnres_read_bwd_noalloc(src, queries, dout, gain=None, eps=1e-6, dsrc=None, accumulate=False,
                              dqueries=None, dgain=None, want_dgain=True, stream=None):
     """attnres_read_bwd with the library's built-in scratch instead of a workspace."""
@@ -310,6 +351,7 @@ def attnres_read_bwd_noalloc(src, queries, dout, gain=None, eps=1e-6, dsrc=None,
     return dsrc, dqueries, dgain
 
 
+@_on_stream
 def attnres_block_phase1_bwd(src, queries, d_o, d_lse=None, gain=None, eps=1e-6, dsrc=None, accumulate=False,
                              dqueries=None, dgain=None, want_dgain=True, workspace=None, stream=None):
     """Backward of Block phase 1 for gradients of its outputs o [n_q,T,d] and
@@ -343,6 +385,7 @@ def attnres_block_phase2_bwd_workspace_size(T, d, dtype):
     return n.value
 
 
+@_on_stream
 def attnres_block_phase2_bwd(o, lse, partial, query, dh, gain=None, eps=1e-6, d_o=None, d_lse=None,
                              d_partial=None, accumulate=False, dquery=None, dgain=None, want_dgain=True,
                              workspace=None, stream=None):
@@ -379,6 +422,7 @@ def mhar_read_bwd_workspace_size(n_src, T, d, H, n_q, dtype):
     return n.value
 
 
+@_on_stream
 def mhar_read_bwd(src, queries, dout, gain=None, eps=1e-6, dsrc=None, accumulate=False, dqueries=None,
                   dgain=None, want_dgain=True, workspace=None, stream=None):
     """Backward of the MHAR read of queries [n_q,H,d/H] over src [n_src,T,d]
@@ -406,6 +450,7 @@ def mhar_read_bwd(src, queries, dout, gain=None, eps=1e-6, dsrc=None, accumulate
     return dsrc, dqueries, dgain
 
 
+@_on_stream
 def mhar_fwd(src, queries, gain=None, eps=1e-6, out=None, lse=None, want_lse=False, stream=None):
     """MHAR: queries [n_q,H,d/H] -> out [n_q,T,d] (lse [n_q,H,T])."""
     import torch
@@ -421,6 +466,7 @@ def mhar_fwd(src, queries, gain=None, eps=1e-6, out=None, lse=None, want_lse=Fal
     return (out, lse) if want_lse else out
 
 
+@_on_stream
 def msar_expand_fwd(src, ksizes, conv_w, queries, gain=None, eps=1e-6, mix_gain=None, mix_w=None,
                     mix_eps=1e-6, out=None, stream=None):
     """MSAR: src [n_src,T,d], ksizes (m-1 ints, host), conv_w packed, queries [m,d],
@@ -457,6 +503,7 @@ def attnres_debug_set_kernel_variant(variant: int):
     load().attnres_debug_set_kernel_variant(int(variant))
 
 
+@_on_stream
 def msar_expand_fwd_chunk(src, t_prev, ksizes, conv_w, queries, gain=None, eps=1e-6, mix_gain=None, mix_w=None,
                           mix_eps=1e-6, out=None, stream=None):
     """MSAR for one chunk: src [n_src, t_prev + T, d] (t_prev history rows first)
@@ -474,6 +521,7 @@ def msar_expand_fwd_chunk(src, t_prev, ksizes, conv_w, queries, gain=None, eps=1
     return out
 
 
+@_on_stream
 def msar_block_phase1(src, ksizes, conv_w, queries, gain=None, eps=1e-6, o=None, lse=None, stream=None):
     """MSAR two-phase, phase 1: queries [S, m, d] of a block's layers over the
     cached sources src [n_src, T, d] -> (o [S, m, T, d], lse [S, m, T])."""
@@ -491,6 +539,7 @@ def msar_block_phase1(src, ksizes, conv_w, queries, gain=None, eps=1e-6, o=None,
     return o, lse
 
 
+@_on_stream
 def msar_block_phase2(o, lse, partial, ksizes, conv_w, query, gain=None, eps=1e-6, mix_gain=None, mix_w=None,
                       mix_eps=1e-6, out=None, stream=None):
     """MSAR two-phase, phase 2 of one layer: o [m, T, d], lse [m, T], partial
@@ -506,6 +555,7 @@ def msar_block_phase2(o, lse, partial, ksizes, conv_w, query, gain=None, eps=1e-
     return out
 
 
+@_on_stream
 def msar_expand_fwd_ps(src, ksizes, conv_w, queries, gain=None, eps=1e-6, mix_gain=None, mix_w=None, mix_eps=1e-6,
                        out=None, stream=None):
     """MSAR with each source's own conv kernels: conv_w [n_src, d*sum(k)] (or
@@ -532,6 +582,7 @@ def msar_expand_bwd_workspace_size(n_src, T, d, dtype, ksizes):
     return n.value
 
 
+@_on_stream
 def msar_expand_bwd(src, ksizes, conv_w, queries, dh, gain=None, eps=1e-6, mix_gain=None, mix_w=None, mix_eps=1e-6,
                     dsrc=None, want_dgain=True, want_dmix_gain=True, grads=None, workspace=None, stream=None):
     """Backward of msar_expand_fwd for dh [T,d] -> (dsrc [n_src,T,d], dconv_w
@@ -564,6 +615,7 @@ def msar_expand_bwd(src, ksizes, conv_w, queries, dh, gain=None, eps=1e-6, mix_g
     return dsrc, dconv_w, dqueries, dgain, dmix_gain, dmix_w
 
 
+@_on_stream
 def msar_expand_bwd_ps(src, ksizes, conv_w, queries, dh, gain=None, eps=1e-6, mix_gain=None, mix_w=None,
                        mix_eps=1e-6, dsrc=None, want_dgain=True, want_dmix_gain=True, grads=None, workspace=None,
                        stream=None):
@@ -606,6 +658,7 @@ def msar_expand_fwd_ws_workspace_size(n_src, T, d, dtype):
     return n.value
 
 
+@_on_stream
 def msar_expand_bwd_chunk(src, t_prev, ksizes, conv_w, queries, dh, dsrc, grads, accumulate, gain=None, eps=1e-6,
                           mix_gain=None, mix_w=None, mix_eps=1e-6, workspace=None, stream=None):
     """Backward of one chunk: src [n_src, t_prev + T, d] (t_prev history rows
@@ -630,6 +683,7 @@ def msar_expand_bwd_chunk(src, t_prev, ksizes, conv_w, queries, dh, dsrc, grads,
     return dsrc
 
 
+@_on_stream
 def msar_expand_fwd_ws(src, ksizes, conv_w, queries, gain=None, eps=1e-6, mix_gain=None, mix_w=None, mix_eps=1e-6,
                        out=None, workspace=None, stream=None):
     """MSAR read through the workspace chain.  conv_w: packed 1-D (shared
@@ -660,6 +714,7 @@ def msar_block_phase1_ws_workspace_size(n_src, T, d, dtype, S):
     return n.value
 
 
+@_on_stream
 def msar_block_phase1_ws(src, ksizes, conv_w, queries, gain=None, eps=1e-6, o=None, lse=None, workspace=None,
                          stream=None):
     """MSAR phase 1 through the workspace chain: queries [S, m, d] ->
@@ -689,6 +744,7 @@ def msar_block_phase2_ws_workspace_size(T, d, dtype):
     return n.value
 
 
+@_on_stream
 def msar_block_phase2_ws(o, lse, partial, ksizes, conv_w, query, gain=None, eps=1e-6, mix_gain=None, mix_w=None,
                          mix_eps=1e-6, out=None, workspace=None, stream=None):
     """MSAR phase 2 of one layer through the workspace chain: o [m, T, d],
@@ -708,6 +764,7 @@ def msar_block_phase2_ws(o, lse, partial, ksizes, conv_w, query, gain=None, eps=
     return out
 
 
+@_on_stream
 def msar_block_phase2_bwd(o, lse, partial, ksizes, conv_w, query, dh, gain=None, eps=1e-6, mix_gain=None, mix_w=None,
                           mix_eps=1e-6, outs=None, workspace=None, stream=None):
     """Backward of msar_block_phase2 for dh [T, d] -> (d_o [m,T,d], d_lse
@@ -738,6 +795,7 @@ def msar_block_phase2_bwd(o, lse, partial, ksizes, conv_w, query, dh, gain=None,
     return d_o, d_lse, d_p, dcw, dq, dg, dmg, dmw
 
 
+@_on_stream
 def msar_block_phase1_bwd(src, ksizes, conv_w, queries, d_o, d_lse, gain=None, eps=1e-6, outs=None, workspace=None,
                           stream=None):
     """Backward of msar_block_phase1 for d_o [S,m,T,d], d_lse [S,m,T] ->
@@ -841,6 +899,7 @@ def _rows(fn, cache):
     return _cuda(fn, cache)
 
 
+@_on_stream
 def attnres_cache_quant(src, fmt, H=1, f=None, cache=None, stream=None):
     """Quantise src [n_src,T,d] (plus f, like src) into cache rows: cache uint8
     [n_src,T,row_bytes], allocated here unless given (sources may be strided)."""
@@ -863,6 +922,7 @@ def attnres_cache_quant(src, fmt, H=1, f=None, cache=None, stream=None):
     return cache
 
 
+@_on_stream
 def attnres_cache_dequant(cache, fmt, d, H=1, dtype=None, out=None, stream=None):
     """Values of cache rows [n_src,T,row_bytes] as dtype (bfloat16) -> [n_src,T,d]."""
     fn = "attnres_cache_dequant"
@@ -879,6 +939,7 @@ def attnres_cache_dequant(cache, fmt, d, H=1, dtype=None, out=None, stream=None)
     return out
 
 
+@_on_stream
 def attnres_cache_read(cache, fmt, queries, gain=None, eps=1e-6, dtype=None, out=None, lse=None, want_lse=True,
                        stream=None):
     """The depth read over a quantised cache [n_src,T,row_bytes]: queries [n_q,d]
@@ -916,6 +977,7 @@ def attnres_cache_read(cache, fmt, queries, gain=None, eps=1e-6, dtype=None, out
 Phase2Norm = collections.namedtuple("Phase2Norm", "codes scales partial h")
 
 
+@_on_stream
 def attnres_phase2_norm_q8(o, lse, partial, query, norm_gain=None, f=None, gain=None, eps=1e-6, norm_eps=1e-6, group=0,
                            partial_out=None, want_h=False, h=None, codes=None, scales=None, stream=None):
     """Phase 2 and the sublayer's RMSNorm in 8 bits: o [T,d], lse [T] or [H,T],
@@ -988,6 +1050,7 @@ def attnres_norm_bwd_workspace_size(T, d, dtype):
     return _norm_bwd_workspace_size(T, d, BF16 if dtype == torch.bfloat16 else F32, torch.cuda.current_device())
 
 
+@_on_stream
 def attnres_norm_bwd(h, dy, gain=None, eps=1e-6, dres=None, dh=None, dgain=None, workspace=None, stream=None):
     """Backward of the sublayer's RMSNorm for h, dy [T,d] (dres [T,d]: the gradient
     past the norm) -> (dh [T,d], dgain [d]).  The workspace is allocated here
