@@ -114,13 +114,13 @@ __device__ __forceinline__ uint32_t e2m1x8(float2 a, float2 b, float2 c, float2 
     return w;
 }
 
-// f32 quotients: v is the correctly rounded quotient and res its residual's sign.  If it is
-// not exact, its last bit is made odd in the residual's direction; borders are even, so it
+// f32 quotients: v is the correctly rounded quotient, negated, and res the quotient's residual.  If
+// it is not exact, its last bit is made odd in the residual's direction; borders are even, so it
 // neither stays on one nor reaches one.
 __device__ __forceinline__ float odd_quotient(float v, float res) {
     const uint32_t b = __float_as_uint(v);
     if (res == 0.f || (b & 1u) || (b << 1) == 0u) return v;
-    return __uint_as_float(((__float_as_uint(res) ^ b) >> 31) ? b - 1u : b + 1u);
+    return __uint_as_float(((__float_as_uint(res) ^ b) >> 31) ? b + 1u : b - 1u);
 }
 
 // Codes of a unit (FP4 with block scale s, S = s 2^k; FP8 with inv = 2^-k), written to p;
@@ -130,18 +130,20 @@ __device__ __forceinline__ float odd_quotient(float v, float res) {
 // product with 1 / S and a residual step round it correctly; its borders have 3 bits, times
 // s's 4, so a quotient on a border is exactly that.  One that only rounds to a border is
 // impossible for bf16 sources (8 bits against 7: at least 2^-8 of it away); for f32 sources
-// the quotient is made odd where it is inexact.
+// the quotient is made odd where it is inexact.  Quotients are formed with their signs turned round:
+// where x is -0 (or +0) the product with -1 / S is +0 (-0) and the residual +0, which times -1 / S
+// leaves that sign in the sum; added as it is to a product of -0 it would not.
 template <typename Tin, int FMT>
 __device__ __forceinline__ float unit_codes(const Unit<Tin> &x, unsigned char *p, float s, float S, float inv) {
     if constexpr (FMT == CACHE_FP4) {
         const float R = S > 0.f ? (Elem<Tin>::BYTES == 2 ? __fdividef(1.f, s) * inv : 1.f / s * inv) : 0.f;
-        const float2 R2 = make_float2(R, R), nS = make_float2(-S, -S);
+        const float2 nR = make_float2(-R, -R), S2 = make_float2(S, S);
         float2 q[8];
         uint32_t low = 1;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const float2 v = x.pair(k), a = fmul2(v, R2);
-            q[k] = ffma2(ffma2(a, nS, v), R2, a);
+            const float2 v = x.pair(k), a = fmul2(v, nR);
+            q[k] = ffma2(ffma2(a, S2, v), nR, a);
             if constexpr (Elem<Tin>::BYTES == 4)
                 low = min(low, min(__float_as_uint(q[k].x) & 0x1fffffu, __float_as_uint(q[k].y) & 0x1fffffu));
         }
@@ -149,11 +151,11 @@ __device__ __forceinline__ float unit_codes(const Unit<Tin> &x, unsigned char *p
             // some quotient has no more than the 3 bits of a border
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                const float2 e = ffma2(q[k], nS, x.pair(k));
+                const float2 e = ffma2(q[k], S2, x.pair(k));
                 q[k] = make_float2(odd_quotient(q[k].x, e.x), odd_quotient(q[k].y, e.y));
             }
         }
-        uint32_t w[2] = {e2m1x8(q[0], q[1], q[2], q[3]), e2m1x8(q[4], q[5], q[6], q[7])};
+        uint32_t w[2] = {e2m1x8(q[0], q[1], q[2], q[3]) ^ 0x88888888u, e2m1x8(q[4], q[5], q[6], q[7]) ^ 0x88888888u};
         __half2 sq = __float2half2_rn(0.f);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
