@@ -16,10 +16,11 @@
 //
 // The codes are unpacked straight into mma.sync.m16n8k16 fragments (f16 inputs,
 // float accumulation): code * s_b is exact in f16, the row scale 2^k and the
-// rms join as factors of a whole row.  The queries, and for float outputs the
-// weights, are split into f16 hi + lo parts (22 significant bits).  For bf16
-// outputs a weight is one f16 (2^-11, an eighth of the output's own rounding):
-// half of pass 2's MMAs, 201 -> 187 us (4 queries, 8 FP8 sources, T = 16384, d = 4096, H = 8).
+// rms join as factors of a whole row.  The queries and the weights are split into f16
+// hi + lo parts (22 significant bits), for bf16 outputs too: with a weight of one f16, off
+// by 2^-12 of it, an output much smaller than its terms loses its bits (5% of outputs
+// left the bf16 value that they round to; now one in thousands).  The lo parts' MMAs cost 5%
+// with FP4 rows (8 sources, T = 32768 269 -> 284 us; 61 sources 255 -> 275 us) and nothing with FP8.
 //   pass 1:  D = X Q, X = [16 rows x 16 channels].  The channel order of a dot
 //            is free, so a lane's fragments come from the 16-byte pieces that it
 //            loads itself; Q (registers, loaded once) has the same order.
@@ -367,10 +368,10 @@ __device__ __forceinline__ int cm_group(int g, int z, int r) {
 // Pass 2 over 8 rows: p0, p1 are the shared addresses of this lane's first group in
 // rows 2c and 2c + 1, q0, q1 those of its scale bytes; whi, wlo the
 // fragment word of the weights of rows 2c, 2c + 1 and query g & 3, in f16 hi and lo
-// parts (LO: whether lo is used).  acc[j]: channel j of the groups of set c / 2, row
+// parts.  acc[j]: channel j of the groups of set c / 2, row
 // 0 (elements 0, 1) and row 1 (elements 2, 3), queries 2c and 2c + 1 mod 4.  FIRST:
 // acc is overwritten.
-template <int FMT, bool FIRST, bool LO>
+template <int FMT, bool FIRST>
 __device__ __forceinline__ void cm_pass2(uint32_t p0, uint32_t p1, uint32_t q0, uint32_t q1, int g, uint32_t whi,
                                          uint32_t wlo, float (&acc)[8][4]) {
     const uint32_t h0 = g < 4 ? whi : 0u, h1 = g < 4 ? 0u : whi;
@@ -378,7 +379,7 @@ __device__ __forceinline__ void cm_pass2(uint32_t p0, uint32_t p1, uint32_t q0, 
     auto step = [&](float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
         if constexpr (FIRST) mma_f16_zero(d, a0, a1, a2, a3, h0, h1);
         else mma_f16(d, a0, a1, a2, a3, h0, h1);
-        if constexpr (LO) mma_f16(d, a0, a1, a2, a3, l0, l1);
+        mma_f16(d, a0, a1, a2, a3, l0, l1);
     };
     if constexpr (FMT == CACHE_FP4) {
         // words 4g .. 4g + 3: (set, row) = (0, 0), (0, 1), (1, 0), (1, 1); one scale per set
@@ -482,11 +483,10 @@ __device__ __forceinline__ void cm_store(unsigned char *o, int64_t qs, int nq, i
     }
 }
 
-// A weight's f16 parts: hi at `a`, lo (LO) `lo` bytes further.
-template <bool LO>
+// A weight's f16 parts: hi at `a`, lo `lo` bytes further.
 __device__ __forceinline__ void cm_put_weight(uint32_t a, uint32_t lo, float w) {
     cm_sts_h(a, w);
-    if constexpr (LO) cm_sts_h(a + lo, w - __half2float(__float2half_rn(w)));
+    cm_sts_h(a + lo, w - __half2float(__float2half_rn(w)));
 }
 
 // The same over n warps' (CL), whole float4s first if they are aligned.
@@ -532,10 +532,11 @@ __device__ __forceinline__ float cm_pow2(float x) { return __uint_as_float(__flo
 __device__ __forceinline__ float cm_inv_pow2(float p) { return __uint_as_float(0x7f000000u - __float_as_uint(p)); }
 
 // The weights alpha * 2^k of a query are taken in units that bring the largest to
-// [2^14, 2^15): it and every weight down to 2^-28 of it (2^-17 with a lo part) is a
-// normal f16, kept to its 11 (22) bits; below that the error is 2^-25 units, 2^-39 of
+// [2^14, 2^15) where a token has at most 8 sources: it and every weight down to 2^-17 of it is
+// kept to 22 bits (its lo part is a normal f16); below that the error is 2^-25 units, 2^-39 of
 // the largest weight (a channel in which every heavier source is exactly zero shows it,
-// nothing else does).
+// nothing else does).  Past 8 sources the largest weight of a reference starts at 2^8 to 2^9 units
+// (cm_form16), so that later ones have room: 22 bits down to 2^-11 of it, then 2^-33 of it.
 constexpr float CM_WEIGHT_TOP = 16384.f;
 
 // What a warp works on.
@@ -803,7 +804,6 @@ struct CMLane {
 
 // Weights of token k of an item and a head, at most 8 sources; lane 8 q + i: query q,
 // source i.  dt: its dot.  lse: this CTA writes it.
-template <bool LO>
 __device__ __forceinline__ void cm_form8(const CacheReadMmaArgs &a, uint32_t st, int k, int head, int64_t t, float dt,
                                          float inv_dh, int lane, bool lse, uint32_t flag) {
     const int q = lane >> 3, i = lane & 7, H = a.r.row.H;
@@ -817,7 +817,7 @@ __device__ __forceinline__ void cm_form8(const CacheReadMmaArgs &a, uint32_t st,
     const float sum = seg_sum<8>(e);
     const float w = on ? __fdividef(e, sum) * cs : 0.f;
     const float p2 = cm_pow2(seg_max<8>(w));
-    cm_put_weight<LO>(w0 + (uint32_t)(((k * H + head) * 4 + q) * 8 + i) * 2, CM_WEIGHT_BYTES * H,
+    cm_put_weight(w0 + (uint32_t)(((k * H + head) * 4 + q) * 8 + i) * 2, CM_WEIGHT_BYTES * H,
                       w * (cm_inv_pow2(p2) * CM_WEIGHT_TOP));
     if (i == 0) {
         cm_sts(f0 + (uint32_t)((k * H + head) * 4 + q) * 4, p2 * (1.f / CM_WEIGHT_TOP));
@@ -830,7 +830,6 @@ __device__ __forceinline__ void cm_form8(const CacheReadMmaArgs &a, uint32_t st,
 // of pass 1.  Row 8 k + i of a stage holds source i of token k.
 template <typename Tout, int FMT, bool CL>
 __global__ void __launch_bounds__(CM_MAX_WARPS * 32, 1) cache_read_mma_kernel(const CacheReadMmaArgs a) {
-    constexpr bool LO = Elem<Tout>::BYTES == 4;
     extern __shared__ __align__(128) unsigned char smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const int n_src = a.r.n_src, H = a.r.row.H;
@@ -915,11 +914,11 @@ __global__ void __launch_bounds__(CM_MAX_WARPS * 32, 1) cache_read_mma_kernel(co
             for (int k = 0; k < 2; ++k) {
                 if (k == 1 && it - a.lag == single) break;
                 const uint32_t whi = cm_lds32(wa + 64 * H * k);
-                const uint32_t wlo = LO ? cm_lds32(wa + 64 * H * k + CM_WEIGHT_BYTES * H) : 0u;
+                const uint32_t wlo = cm_lds32(wa + 64 * H * k + CM_WEIGHT_BYTES * H);
                 const float2 m = cm_lds64f(fa + 16 * H * k);
                 float acc[8][4];
                 const uint32_t x = r2.base + at.p2 + 8 * k * a.pitch, y = r2.base + at.q2 + 8 * k * a.pitch;
-                cm_pass2<FMT, true, LO>(x, x + a.pitch, y, y + a.pitch, g, whi, wlo, acc);
+                cm_pass2<FMT, true>(x, x + a.pitch, y, y + a.pitch, g, whi, wlo, acc);
                 if (live) cm_store<Tout, FMT, true>(out + k * tok_bytes, a.r.out_q_stride_bytes, at.nq, at.rows, a.wide, acc, m);
             }
             __syncwarp();
@@ -952,7 +951,7 @@ __global__ void __launch_bounds__(CM_MAX_WARPS * 32, 1) cache_read_mma_kernel(co
                 for (int k = 0; k < 2; ++k)
                     if (k == 0 ? forms0 : forms1) {
                         if constexpr (CL) dt[k] = cm_all_sums(a, sl, share, r1.base, k, dt[k], lane);
-                        cm_form8<LO>(a, r1.base, k, head, 2 * (bid + (int64_t)it * gstride) + k, dt[k], inv_dh, lane, lse, flag);
+                        cm_form8(a, r1.base, k, head, 2 * (bid + (int64_t)it * gstride) + k, dt[k], inv_dh, lane, lse, flag);
                     }
                 __syncwarp();
                 if (lane == 0) cm_arrive(r1.base + weights_in);
@@ -971,7 +970,6 @@ __global__ void __launch_bounds__(CM_MAX_WARPS * 32, 1) cache_read_mma_kernel(co
 // Weights of 16 rows (one item) of a token and head, and the factor by which what
 // is summed so far is to be rescaled; lane 8 q + i: query q, rows i and 8 + i.  state:
 // the token's reference score, sum and unit, 4 queries each.  dt: the dots.
-template <bool LO>
 __device__ __forceinline__ void cm_form16(const CacheReadMmaArgs &a, uint32_t st, int head, int64_t t, int chunk, bool last,
                                           const float (&dt)[2], float inv_dh, int lane, bool lse, uint32_t state, uint32_t flag) {
     const int q = lane >> 3, i = lane & 7, H = a.r.row.H;
@@ -1015,8 +1013,8 @@ __device__ __forceinline__ void cm_form16(const CacheReadMmaArgs &a, uint32_t st
     l += seg_sum<8>(e0 + e1);
     const float iu = cm_inv_pow2(u);
     const uint32_t w = w0 + (uint32_t)((head * 4 + q) * 16 + i) * 2;
-    cm_put_weight<LO>(w, CM_WEIGHT_BYTES * H, on[0] ? e0 * cs[0] * iu : 0.f);
-    cm_put_weight<LO>(w + 16, CM_WEIGHT_BYTES * H, on[1] ? e1 * cs[1] * iu : 0.f);
+    cm_put_weight(w, CM_WEIGHT_BYTES * H, on[0] ? e0 * cs[0] * iu : 0.f);
+    cm_put_weight(w + 16, CM_WEIGHT_BYTES * H, on[1] ? e1 * cs[1] * iu : 0.f);
     __syncwarp();
     if (i == 0) {
         cm_sts(state + 4 * q, m);
@@ -1038,7 +1036,6 @@ __device__ __forceinline__ void cm_form16(const CacheReadMmaArgs &a, uint32_t st
 // item's factor rescales them when it moves the reference (cm_form16).
 template <typename Tout, int FMT, bool CL>
 __global__ void __launch_bounds__(CM_MAX_WARPS * 32, 1) cache_read_mma_multi_kernel(const CacheReadMmaArgs a) {
-    constexpr bool LO = Elem<Tout>::BYTES == 4;
     extern __shared__ __align__(128) unsigned char smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const int n_src = a.r.n_src, H = a.r.row.H, nchunks = (n_src + CM_ROWS - 1) / CM_ROWS;
@@ -1136,9 +1133,9 @@ __global__ void __launch_bounds__(CM_MAX_WARPS * 32, 1) cache_read_mma_multi_ker
             }
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const uint32_t whi = cm_lds32(wa + 16 * k), wlo = LO ? cm_lds32(wa + 16 * k + CM_WEIGHT_BYTES * H) : 0u;
+                const uint32_t whi = cm_lds32(wa + 16 * k), wlo = cm_lds32(wa + 16 * k + CM_WEIGHT_BYTES * H);
                 const uint32_t x = r2.base + at.p2 + 8 * k * a.pitch, y = r2.base + at.q2 + 8 * k * a.pitch;
-                cm_pass2<FMT, false, LO>(x, x + a.pitch, y, y + a.pitch, g, whi, wlo, acc);
+                cm_pass2<FMT, false>(x, x + a.pitch, y, y + a.pitch, g, whi, wlo, acc);
             }
             if (++chunk_p == nchunks) {
                 if (!cm_aborted(flag))
@@ -1178,7 +1175,7 @@ __global__ void __launch_bounds__(CM_MAX_WARPS * 32, 1) cache_read_mma_multi_ker
 #pragma unroll
                     for (int k = 0; k < 2; ++k) dt[k] = cm_all_sums(a, sl, share, r1.base, k, dt[k], lane);
                 }
-                cm_form16<LO>(a, r1.base, head, t, chunk, chunk == nchunks - 1, dt, inv_dh, lane, lse, flag + CM_STATE + 48 * head,
+                cm_form16(a, r1.base, head, t, chunk, chunk == nchunks - 1, dt, inv_dh, lane, lse, flag + CM_STATE + 48 * head,
                               flag);
                 __syncwarp();
                 if (lane == 0) cm_arrive(r1.base + weights_in);
