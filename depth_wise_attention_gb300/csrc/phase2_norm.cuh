@@ -322,7 +322,9 @@ __global__ void __launch_bounds__(PN_THREADS, VPT <= 2 ? (MODE == PN_MERGE ? 2 :
             }
         }
         const float ms = fmaf(ss, inv_d, a.norm_eps);
-        const float rr = ms > 0.f ? rsqrtf(ms) : ms;        // a zero row with eps = 0 is zero; NaN stays
+        // a zero row with eps = 0 is zero; a NaN stays, and infinity makes one: it is the whole row's, also
+        // of the groups that are finite themselves
+        const float rr = (ms > 0.f ? rsqrtf(ms) : ms) + (ms - ms);
         if (a.group == 0) {
             const float iv = code_factor(rmax);
             if (tr == 0 && row_ok) a.scales[t] = rmax * rr * (1.f / 448.f);

@@ -848,9 +848,9 @@ attnres_status_t attnres_cache_read(const void *cache, int64_t n_src, int64_t ca
  *   scale = max|y| / 448 per row (group = 0) or per group of 32, 64 or 128
  *   channels, code = e4m3(y / scale), to nearest even
  * All of it in float32 on p' and h before any rounding.  A row (or group) whose
- * max|norm_gain * h| is below 1e-35 has codes 0; one with a NaN, or a row whose
- * h is infinite, has a NaN scale.  Where lse = -inf nothing was read and h = p'
- * whatever o holds.
+ * max|norm_gain * h| is below 1e-35 has codes 0.  A row whose h has a NaN or an
+ * infinity, or whose mean(h^2) is beyond float's range, has NaN scales, those of
+ * all its groups.  Where lse = -inf nothing was read and h = p' whatever o holds.
  *   partial_out  [T][d] dtype dt, required with f: p' rounded once; may be
  *                partial or f itself.  Without f it is not written
  *   lse, query, gain, eps  the merge's ([H][T], [d], [d] or NULL); ignored when
