@@ -986,7 +986,8 @@ __device__ __forceinline__ void cm_form16(const CacheReadMmaArgs &a, uint32_t st
         score[k] = on[k] ? cm_score(dt[k], ss, inv_dh, a.r.eps, cs[k]) : -INFINITY;
     }
     // Weights e^(s - m) c in units u against the reference (m, u) of the items so far, unless one
-    // of them passes f16 there: then the reference moves to this item's largest score and weight,
+    // of them passes f16 there, or e^(s - m) itself passes 2^75 (rows of tiny scale: the sum would
+    // pass float before a weight passes f16): then the reference moves to this item's largest score and weight,
     // and the sums are rescaled.  The largest weight of a reference starts at 2^8 to 2^9 units, so
     // that is rare (rescaling at every new maximum: 314 us, so: 302; 61 sources, T = 4099).
     // Nothing lies below 2^-110: row scales do not.
@@ -995,7 +996,9 @@ __device__ __forceinline__ void cm_form16(const CacheReadMmaArgs &a, uint32_t st
     const float top = seg_max<8>(fmaxf(score[0], score[1]));
     float e0 = on[0] ? __expf(score[0] - m) : 0.f, e1 = on[1] ? __expf(score[1] - m) : 0.f;
     float f = 1.f;
-    const bool move = chunk == 0 || seg_max<8>(fmaxf(on[0] ? e0 * cs[0] : 0.f, on[1] ? e1 * cs[1] : 0.f)) > 60000.f * u;
+    const float least = u * 0x1p-60f;
+    const bool move = chunk == 0 || seg_max<8>(fmaxf(on[0] ? e0 * fmaxf(cs[0], least) : 0.f,
+                                                     on[1] ? e1 * fmaxf(cs[1], least) : 0.f)) > 60000.f * u;
     if (__any_sync(0xffffffffu, move)) {
         const float mn = fmaxf(m, top), keep = chunk == 0 ? 0.f : __expf(m - mn);
         const float n0 = on[0] ? __expf(score[0] - mn) : 0.f, n1 = on[1] ? __expf(score[1] - mn) : 0.f;
