@@ -2283,8 +2283,8 @@ constexpr size_t kCacheSmemSlack = 4096;
 constexpr size_t kCacheNarrowSmem = 64 * 1024; // queries and weights of the narrow-head read, per CTA
 // The few-token read's cost goes with its CTAs and their sources, the streaming kernel's
 // first item costs 10 to 17 us.  Measured (few against streaming, us): d = 4096, 8 sources,
-// 1 token 5.0 / 9.4, 64 tokens 10.5 / 10.3, 128 tokens 18.7 / 10.3; 61 sources, 1 token
-// 10.6 / 17.2, 64 tokens 29.9 / 17.6.
+// 1 token 4.7 / 9.6, 64 tokens 10.0 / 10.4, 128 tokens 18.7 / 10.3; 61 sources, 1 query, 1 token
+// 10.4 / 17.0, 64 tokens 29.9 / 17.6.
 constexpr int64_t kCacheFewWork = 20480;       // tokens * CTAs a token * (32 + sources)
 
 // Scalars and layout shared by the cache entry points.  The cache holds
@@ -2637,7 +2637,9 @@ attnres_status_t launch_cache_read(const void *cache, int64_t n_src, int64_t cac
         if (st != ATTNRES_OK || done) return st;
     }
     if (kv != 1) {
-        // the tensor-core kernels take 4 queries at a time: the rows are a fraction of the outputs
+        // the tensor-core kernels take 4 queries at a time, so 5 to 8 read the rows twice.  With 8 sources the
+        // rows are at most half of what 4 queries move; past that they are most of it (61 FP4 sources 35
+        // bytes a channel, 4 bf16 outputs 8), and two launches cost nearly two reads
         bool done = true;
         for (int64_t q0 = 0; q0 < n_q && done; q0 += 4) {
             CacheReadArgs r = a;

@@ -48,14 +48,16 @@
 // take turns at the weights: with the same warp every time that warp's three jobs set
 // the pace (334 -> 304 us; 4 queries, 8 FP4 sources, T = 32768, d = 4096).  Dots and
 // weights lie in the item's stage, so its ring is the only counter, and every
-// offset of a lane inside a stage is computed once (304 -> 280 us): what bounds the
-// read is the issue of its instructions, about 200 a warp and item in pass 1 and 240
-// in pass 2, half of them unpacking, plus some 150 around them.
-// Measured with bf16 outputs, 4 queries, d = 4096: 8 FP4 sources, T = 32768, 272 us
-// (6.2 TB/s); 8 FP8 sources, T = 32768, 338 us (6.4 TB/s); the same with H = 8, T = 16384,
-// 176 us (6.1 TB/s); 61 FP4 sources, T = 4099, 280 us (2.6 TB/s: codes of half a byte are
-// unpacked twice, and hardly anything is written beside them).  On clusters, d = 8192, T =
-// 8192, 8 FP4 sources 177 us (4.8 TB/s), 8 FP8 sources 177 us (6.1 TB/s).
+// offset of a lane inside a stage is computed once (304 -> 280 us).  With 8 sources HBM and
+// the issue of instructions bound the read: of 730 a warp and item (two tokens of 8 FP4 sources) some
+// 200 in pass 1 and 260 in pass 2, most of these unpacking.  Past 8 sources nothing is full (61 FP4
+// sources: issue slots 58%, ALU pipe 45%, tensor pipe 31%, HBM 26%): one CTA of 16 warps at 128
+// registers, of which a few spill (up to 40 bytes), does not hide its latencies; every byte is
+// unpacked twice; and with one query three of pass 2's four query columns are zeros.
+// Measured with bf16 outputs, 4 queries, d = 4096: 8 FP4 sources, T = 32768, 284 us
+// (5.9 TB/s); 8 FP8 sources, T = 32768, 330 us (6.5 TB/s); the same with H = 8, T = 16384,
+// 178 us (6.1 TB/s); 61 FP4 sources, T = 4099, 282 us, 1 query 275 (2.2 TB/s).  On clusters,
+// d = 8192, T = 8192, 8 FP4 sources 189 us (4.4 TB/s), 8 FP8 sources 182 us (5.9 TB/s).
 #pragma once
 
 #include "depth_cache.cuh"

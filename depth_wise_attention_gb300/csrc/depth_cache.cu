@@ -197,10 +197,10 @@ __device__ __forceinline__ float unit_codes(const Unit<Tin> &x, unsigned char *p
 // take two units a thread where they have them: much of a row's work goes by threads.  One
 // CTA barrier a row: the sums of squares and the row's tail are finished behind the next row's.
 // Memory: 2 or 4 bytes a channel in (twice with f), 0.5625 or 1 out.  Partial + output, bf16
-// -> FP4, 32768 x 4096: 163 us with a CTA per row and two barriers, 95 (floor 91).
+// -> FP4, 32768 x 4096: 163 us with a CTA per row and two barriers, 92 (floor 90).
 // Registers are the limit of the CTAs per SM: words of a thread's units, twice with f.  A CTA has
 // whole rows' threads (at most CACHE_THREADS), so no warp idles: f32 -> FP4, 12297 x 1056 27.0 ->
-// 23.9 us.
+// 23.9 us (22.6 now; 32768 x 4096 123, floor 90: the exact quotients of every channel).
 template <typename Tin, int FMT, int UPT, bool ADD>
 __global__ void __launch_bounds__(CACHE_THREADS, UPT * Elem<Tin>::BYTES <= 2 ? 4 : UPT * Elem<Tin>::BYTES <= 4 ? (ADD ? 2 : 3) : 1)
     cache_quant_kernel(const CacheQuantArgs a) {
@@ -299,8 +299,9 @@ __global__ void __launch_bounds__(CACHE_THREADS, UPT * Elem<Tin>::BYTES <= 2 ? 4
 }
 
 // Reads cache rows back: value = code * s_b * 2^k, exact in float; bf16 values (at most 6
-// significant bits) are exact too.  HBM-bound: one unit per thread and row, two rows' loads
-// in flight.  FP4 -> bf16, 32768 x 4096: 66 us with a row per CTA, 60 (floor 50).
+// significant bits) are exact too.  HBM-bound: one unit per thread and step, the loads of two
+// units of a row in flight where a thread has as many, other rows' in the SM's other CTAs.  FP4 ->
+// bf16, 32768 x 4096: 66 us with a row per CTA, 57 with persistent ones (floor 50).
 template <typename Tout, int FMT>
 __global__ void __launch_bounds__(CACHE_THREADS) cache_dequant_kernel(const CacheDequantArgs a) {
     using E = Elem<Tout>;
