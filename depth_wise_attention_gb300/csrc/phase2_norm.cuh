@@ -17,10 +17,10 @@
 // barriers a tile (one without a merge).  Bound by HBM where three or four arrays
 // move, by latency for few tokens.  Measured, bf16, 32768 x 4096, codes per row:
 //   residual layer (partial, f)       145 us, 6.5 TB/s
-//   merge (o, partial, f)             198 us, 6.1 TB/s: 2 CTAs an SM at 128 registers
+//   merge (o, partial, f)             194 us, 6.2 TB/s: 2 CTAs an SM at 128 registers
 //   first layer (o)                    89 us, 4.5 TB/s: few bytes a row for its two
 //     reductions; loading two tiles ahead cost 5 us
-// and the backward (h, dy, dres read, dh written) 171 us, 6.3 TB/s; one token 4.6
+// and the backward (h, dy, dres read, dh written) 168 us, 6.4 TB/s; one token 4.6
 // and 5.4 us.  Two sums that a warp needs at once share one chain of shuffles and
 // maxima are compared as integers (merge 211 -> 208 us); one exponential and one division
 // for the two shares, and rsqrtf where it reaches no code directly (208 -> 198 us).
